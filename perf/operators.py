@@ -210,9 +210,6 @@ def prepare(case, seed):
     gen = torch.Generator(device="cuda").manual_seed(seed)
     op = case["op"]
     s = {"op": op}
-    if own and op in ("write", "read"):  # one status word serves a program's calls
-        from mla_decode_attention_03_gb300 import ops
-        s["status"] = ops.new_status()
     if op in ("decode", "read"):
         lengths = _lengths(case)
         pages = [(L + PAGE - 1) // PAGE for L in lengths]
@@ -265,10 +262,10 @@ def _own(s):
                                 causal=s["q"].shape[1] > 1)
         return {"out": out, "lse": lse}
     if s["op"] == "write":
-        ops.write_cache_fp8(s["kv_c"], s["k_pe"], s["slots"], s["cache"], s["scales"], status=s["status"])
+        ops.write_cache_fp8(s["kv_c"], s["k_pe"], s["slots"], s["cache"], s["scales"])
         return {"cache": s["cache"], "scales": s["scales"]}
     if s["op"] == "read":
-        return ops.read_cache_fp8(s["cache"], s["scales"], s["block_table"], s["cu"], s["total"], status=s["status"])
+        return ops.read_cache_fp8(s["cache"], s["scales"], s["block_table"], s["cu"], s["total"])
     q, k = ops.rope(s["q_pe"], s["positions"], s["rotary"], out=s["q_out"][..., LATENT:], k=s["k_pe"], k_out=s["k_out"])
     return {"q": q, "k": k}
 
