@@ -530,8 +530,9 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
         tc_fence_before_sync();
       }
     }
-  } else if (warp == 16) {
-    regs_dec<64>();
+  } else {
+    regs_dec<64>();  // here: all warps of a warpgroup have to execute the same one, and warps 16 and 17 share one
+    if (warp == 16) {
       // ================================================= the other page's half of V; the weights' factors
       const uint64_t evict_first = l2_policy_evict_first();
       const int past = static_cast<int>(P.num_blocks * kPage);
@@ -613,10 +614,7 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
       }
       if (lane == 0)  // the last copies land before this CTA can exit, whoever gave up
         for (int k = max(0, n - kTiles); k < n; ++k) drain_wait(bar(kCrossed + k % kTiles), (k / kTiles) & 1);
-    __syncwarp();
-  } else {
-    regs_dec<64>();
-    if (lane == 0) {
+    } else if (lane == 0) {
       if (warp == 17) {
         // ================================================= the own page
         tma_prefetch_desc(&lat_map);
