@@ -237,8 +237,7 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
   cluster_sync();  // both CTAs' barriers and tensor memory are there
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  // The schedule is there: the queries' kernel, which this launch follows, waited
-  // for it before it let this one start.  The queries and the workspace may not be.
+  grid_dependency_wait();  // the queries, and what came before them: the schedule, the cache
   grid_launch_dependents();
 
   bool ok = true;
@@ -456,7 +455,6 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
 
       // ---- end of a segment: row sums over the eight threads, O out
       if (rare(w.last())) {
-        grid_dependency_wait();  // whatever still reads `out`, `lse` or the workspace
         const int s0 = __ldg(P.num_splits + w.i);
         const bool whole = __ldg(P.num_splits + w.i + 1) - s0 == 1;
         const int64_t out_row = whole ? static_cast<int64_t>(w.i) * rows_total : (static_cast<int64_t>(s0) + w.k) * rows_total;
@@ -664,7 +662,6 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
         }
       } else if (warp == 21) {
         // ================================================= queries
-        grid_dependency_wait();
         TileWalk w;
         w.start(meta, P.cache_seqlens, P.max_blocks);
         int seg = 0;

@@ -1,0 +1,49 @@
+"""Decode over the 8-bit cache where scales are zero, hidden, or anywhere in the type's range, against the definition in
+64 bits.  The bounds are those of _kv8_reference."""
+import math
+
+import pytest
+import torch
+
+from mla_decode_attention_03_gb300 import ops
+from tests._kv8_reference import ENTRY, attention
+from tests.test_kv8_decode import SCALE, decode, held, inputs
+
+gpu = pytest.mark.gpu
+
+
+def at(bt, i, t):
+    """(page, 0, slot) of token t of sequence i in the scales."""
+    return int(bt[i, t // 64]), 0, t % 64
+
+
+@gpu
+@pytest.mark.parametrize("h_q,s_q", [(16, 2), (10, 3), (40, 2), (96, 3), (128, 2)])
+@pytest.mark.parametrize("parts", [None, 1, 40])
+def test_hidden_scales_of_any_value(h_q, s_q, parts):
+    """Whatever scale the last tokens have, the queries that do not see them keep their results, bit for bit."""
+    lens = [300, 63, 1, 2, 129, 190, 65, 128, 700]
+    q, cache, scales, bt, sl = inputs(lens, s_q, h_q, seed=50)
+    first = decode(q, cache, scales, bt, sl, causal=True, parts=parts)
+    held(*first, attention(q, cache, scales, bt, sl, SCALE, True))
+    for value in (0.0, -0.0, 2.0 ** -149, 2.0 ** -126, 3e38, math.nan, math.inf):
+        hidden = scales.clone()
+        for i, L in enumerate(lens):
+            hidden[at(bt, i, L - 1)] = value
+        out, lse = decode(q, cache, hidden, bt, sl, causal=True, parts=parts)
+        assert torch.equal(out[:, :-1], first[0][:, :-1]) and torch.equal(lse[..., :-1], first[1][..., :-1]), value
+        if value < 1:  # the last query sees a key of (almost) zero
+            held(out, lse, attention(q, cache, hidden, bt, sl, SCALE, True))
+
+
+@gpu
+@pytest.mark.parametrize("h_q", [16, 64, 128])
+def test_a_nan_with_a_scale_of_zero_is_seen(h_q):
+    q, cache, scales, bt, sl = inputs([300, 64, 129], 2, h_q, seed=51)
+    first = decode(q, cache, scales, bt, sl, causal=True)
+    for i, L in enumerate((300, 64, 129)):
+        scales[at(bt, i, L - 1)] = 0.0
+        cache.view(torch.uint8)[int(bt[i, (L - 1) // 64]), (L - 1) % 64, 0, 575] = 0x7F
+    out, lse = decode(q, cache, scales, bt, sl, causal=True)
+    assert torch.equal(out[:, 0], first[0][:, 0]) and torch.equal(lse[..., 0], first[1][..., 0])
+    assert torch.isnan(out[:, 1]).all() and torch.isnan(lse[..., 1]).all()
