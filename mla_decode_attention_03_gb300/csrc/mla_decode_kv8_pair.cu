@@ -82,7 +82,7 @@ constexpr int kOffP = kOffQ + kQBytes;
 constexpr int kOffScale = kOffP + 2 * kPBytes;
 constexpr int kOffMx = kOffScale + kScaleSlots * kTile * 4;  // float[2][kSlices][64] partial maxima, and row sums
 constexpr int kOffUnit = kOffMx + 2 * kSlices * kRows * 4;             // float[kScaleSlots][3][128] scales; their part in the weights; its log2
-constexpr int kOffBound = kOffUnit + 3 * kScaleSlots * kTile * 4;  // float[kScaleSlots][2] R, whether a scale is not finite
+constexpr int kOffBound = kOffUnit + 3 * kScaleSlots * kTile * 4;  // float[kScaleSlots][2] R, whether a scale is 0 or not finite
 constexpr int kOffC = kOffBound + kScaleSlots * 8;           // float[kCSlots][64] c_r of the last segments
 constexpr int kOffRow = kOffC + kCSlots * kRows * 4;         // int[64] row in the sequence
 constexpr int kOffBar = kOffRow + kRows * 4;
@@ -292,8 +292,9 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
       const float* const factors = factors_of + (n & 3) * (3 * kTile) + page * kPage + g * 16;
       const float* const bnd = bounds + 2 * (n & 3);
       if (rare(ragged || bnd[1] != 0.f)) {
-        // Scores of hidden tokens become -inf, and those of tokens whose scale is not
-        // finite NaN (their factor is 1), before they are read below.
+        // Before they are read below, scores of hidden tokens become -inf, those of tokens
+        // whose scale is not finite NaN, and those of scale 0 zero: the factor of the last
+        // two is 1, for a hidden one may be among them, and -inf x 0 is NaN.
 #pragma unroll 1
         for (int k = 0; k < 16; k += 8) {
           uint32_t x[8], y[8];
@@ -305,6 +306,10 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             if (!(raw[k + e] < INFINITY)) x[e] = 0x7fffffffu;
+            if (!(raw[k + e] > 0.f)) {  // 0, or NaN
+              x[e] = __float_as_uint((__uint_as_float(x[e]) + __uint_as_float(y[e])) * 0.f);
+              y[e] = 0;
+            }
             if (tok0 + k + e >= lim) {
               x[e] = 0xff800000u;
               y[e] = 0;
@@ -541,8 +546,8 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
       next = w;
       int n = 0, m = 0;
       float bound = 1.f;
-      // The scales (1 past the end and for one that is not finite), kUnit scale / R (0
-      // there), and log2(scale / R).  R is over the tokens that every row sees.  A row that sees a token whose scale is
+      // The scales (1 past the end, and for one that is 0 or not finite), kUnit scale / R (0 there), and
+      // log2(scale / R).  R is over the tokens that every row sees.  A row that sees a token whose scale is
       // not finite gets a NaN score; to the others it is nothing.  Four slots: factors m + 4 are made once S(m + 3) is
       // done, which waits until the softmax has left tile m.
       auto factors = [&]() {
@@ -557,7 +562,7 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
         uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool fine = s[e] < INFINITY;
+          const bool fine = s[e] > 0.f && s[e] < INFINITY;
           odd = odd || (e < end && !fine);
           scale[e] = e < end && fine ? s[e] : 1.f;
           if (!(e < end && fine)) s[e] = 0.f;
