@@ -207,12 +207,12 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
       const float* const sc = scales + (n & 3) * kTile;
       float scale = tok < seg_end ? sc[tl] : 0.f;
       if (!(scale < INFINITY)) scale = __uint_as_float(0x7fffffffu);  // a row that sees it becomes NaN
-      if (rare(first)) {  // R, over the tokens that every row sees
+      if (rare(first)) {  // R, over the tokens that every row sees, and the first: who sees any sees that
         uint32_t top = 0;
 #pragma unroll 1
         for (int e = lane; e < kTile; e += 32) {
           const uint32_t a = __float_as_uint(sc[e]);
-          if (t0 + e < all_see && a < 0x7f800000u) top = max(top, a);
+          if ((t0 + e < all_see || e == 0) && a < 0x7f800000u) top = max(top, a);
         }
         bound = fminf(fmaxf(__uint_as_float(__reduce_max_sync(0xffffffffu, top)), kMinR), kMaxR);
       }

@@ -547,8 +547,9 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
       int n = 0, m = 0;
       float bound = 1.f;
       // The scales (1 past the end, and for one that is 0 or not finite), kUnit scale / R (0 there), and
-      // log2(scale / R).  R is over the tokens that every row sees.  A row that sees a token whose scale is
-      // not finite gets a NaN score; to the others it is nothing.  Four slots: factors m + 4 are made once S(m + 3) is
+      // log2(scale / R).  R is over the tokens that every row sees, and the first, which every row that sees one
+      // of the segment's tokens sees.  A row that sees a token whose scale is not finite gets a NaN score; to the
+      // others it is nothing.  Four slots: factors m + 4 are made once S(m + 3) is
       // done, which waits until the softmax has left tile m.
       auto factors = [&]() {
         ok = warp_wait(bar(kScaleFull + (m & 3)), (m >> 2) & 1, abort_flag);
@@ -566,7 +567,7 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
           odd = odd || (e < end && !fine);
           scale[e] = e < end && fine ? s[e] : 1.f;
           if (!(e < end && fine)) s[e] = 0.f;
-          if (e < all_see) top = max(top, __float_as_uint(s[e]));
+          if (e < all_see || 4 * lane + e == 0) top = max(top, __float_as_uint(s[e]));
         }
         odd = __any_sync(0xffffffffu, odd);
         top = __reduce_max_sync(0xffffffffu, top);

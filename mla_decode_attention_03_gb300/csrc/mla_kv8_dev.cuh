@@ -18,8 +18,8 @@ constexpr int kTile = 128;  // tokens: two pages
 // is near kUnit whatever the scales beside it are, those of tokens that it does not
 // see among them.  M is moved (and O rescaled, between two products) only when it
 // grew by more than kSlack (log2): weights stay below kUnit 2^kSlack < 448, e4m3's
-// largest.  R, the largest scale of the segment's first tile, serves the range only:
-// P and its sum l reach R / scale.
+// largest.  R, the largest scale of the segment's first tile over the tokens that every
+// row sees and the first one, serves the range only: P and its sum l reach R / scale.
 constexpr float kMargin = 1.f;             // a maximum that moves goes this far beyond, so that it moves less often
 constexpr float kMinR = 0x1p-60f, kMaxR = 0x1p120f;
 constexpr float kMaxRatio = 0x1p100f;      // of scale / R

@@ -47,3 +47,19 @@ def test_a_nan_with_a_scale_of_zero_is_seen(h_q):
     out, lse = decode(q, cache, scales, bt, sl, causal=True)
     assert torch.equal(out[:, 0], first[0][:, 0]) and torch.equal(lse[..., 0], first[1][..., 0])
     assert torch.isnan(out[:, 1]).all() and torch.isnan(lse[..., 1]).all()
+
+
+@gpu
+@pytest.mark.parametrize("h_q", [16, 40, 128])
+@pytest.mark.parametrize("s_q", [2, 3, 70])
+def test_few_tokens_at_the_far_end_of_the_range(h_q, s_q):
+    """Lengths where no token, or none of a piece, is seen by every query: one scale decides for those that see it."""
+    if s_q == 70 and h_q != 16:
+        pytest.skip("one shape of many positions is enough")
+    q0, cache, scales0, bt, sl = inputs([1, 2, 65, 129, 200, 3, 64], s_q, h_q, seed=53)
+    for power in (-60, 60, 92, 110):
+        q = (q0.float() * 2.0 ** -power).to(torch.bfloat16)
+        x = (q, cache, scales0 * 2.0 ** power, bt, sl)
+        ref = attention(*x, SCALE, True)
+        for parts in (None, 1, 4, 60):
+            held(*decode(*x, causal=True, parts=parts), ref)
