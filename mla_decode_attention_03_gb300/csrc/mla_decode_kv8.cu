@@ -5,7 +5,7 @@
 //   S[t, r] = c_r scale_t <q'_r, code_t>       c_r = softmax_scale log2(e) 2^e_r
 //   P[t, r] = 2^(S[t, r] - M_r)                M_r the running maximum of S[t, r] + log2(scale_t / R)
 //   O[:, r] = sum_t (P[t, r] scale_t / R) code_t[0:512],   l_r = sum_t P[t, r]
-//   out_r   = R O[:, r] / l_r                  R the first tile's largest scale
+//   out_r   = R O[:, r] / l_r                  R about the first tile's largest scale
 //
 // The codes go to the tensor cores as they lie in the cache: nothing is
 // converted.  The other operand is made of two e4m3 numbers, x = hi + lo, in
@@ -170,7 +170,7 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     float* const mx = reinterpret_cast<float*>(gbase + C::OffMx);
     float* const ls = reinterpret_cast<float*>(gbase + C::OffLs) + g * 128;
-    float* const bc = reinterpret_cast<float*>(gbase + C::OffBc) + warp * 64;  // [0]: -M or 1/l, [1]: rescale factors
+    float* const bc = reinterpret_cast<float*>(gbase + C::OffBc) + warp * 64;  // [0]: -M or 1/l, [1]: roots of l's factors, then O's factors
     const float* const scales = reinterpret_cast<const float*>(gbase + C::OffScale);
     const int rows_total = P.s_q * P.h_q;
 
@@ -207,14 +207,19 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
       const float* const sc = scales + (n & 3) * kTile;
       float scale = tok < seg_end ? sc[tl] : 0.f;
       if (!(scale < INFINITY)) scale = __uint_as_float(0x7fffffffu);  // a row that sees it becomes NaN
-      if (rare(first)) {  // R, over the tokens that every row sees, and the first: who sees any sees that
-        uint32_t top = 0;
+      int shift = 0;                                       // by which log2(R) moves
+      if (rare(first || bound == kMinR)) {
+        uint32_t top = 0, any = 0;
 #pragma unroll 1
         for (int e = lane; e < kTile; e += 32) {
           const uint32_t a = __float_as_uint(sc[e]);
-          if ((t0 + e < all_see || e == 0) && a < 0x7f800000u) top = max(top, a);
+          if (t0 + e >= seg_end || a >= 0x7f800000u) continue;
+          any = max(any, a);
+          if (t0 + e < all_see || e == 0) top = max(top, a);
         }
-        bound = fminf(fmaxf(__uint_as_float(__reduce_max_sync(0xffffffffu, top)), kMinR), kMaxR);
+        const float r = reference_scale(__reduce_max_sync(0xffffffffu, top), __reduce_max_sync(0xffffffffu, any));
+        if (!first) shift = log2_of_power(r) - log2_of_power(bound);
+        bound = r;
       }
       // (a NaN scale counts as 0 here: to a row that does not see it, it is nothing)
       const float ratio = scale < INFINITY ? fminf(scale * (1.f / bound), kMaxRatio) : 0.f;
@@ -260,17 +265,20 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
       if (lane == 0) mbar_arrive(bar(C::Mx + 2 * g + (n & 1)));
       ok = warp_wait(bar(C::Mx + 2 * g + (n & 1)), (n >> 1) & 1, abort_flag);
       if (rare(!ok)) break;
-      float alpha = 1.f;
+      float root = 1.f;  // of the factor by which l moves
       if (lane < H) {
         const float m = fmaxf(fmaxf(mxb[lane], mxb[32 + lane]), fmaxf(mxb[64 + lane], mxb[96 + lane]));
-        if (m > m_run + kSlack) {
-          alpha = ex2_approx(m_run - m);  // 0 from -inf
-          m_run = m;
+        float to = m_run;
+        if (rare(shift != 0) && m != -INFINITY) to -= fminf(static_cast<float>(shift), kMaxLess);
+        if (m > to + kSlack) to = m;
+        if (to != m_run) {
+          root = root_of_move(m_run - to);  // 0 from -inf
+          m_run = to;
         }
         bc[lane] = m_run == -INFINITY ? 0.f : -m_run;
-        bc[32 + lane] = alpha;
+        bc[32 + lane] = root;
       }
-      const bool moved = __any_sync(0xffffffffu, alpha != 1.f);
+      const bool moved = __any_sync(0xffffffffu, root != 1.f || shift != 0);
       __syncwarp();
 
       // ---- weights: hi and lo bytes of four rows a register
@@ -278,7 +286,7 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
       uint32_t ph[H / 4], pl[H / 4];
       if (moved) {
 #pragma unroll
-        for (int r = 0; r < H; ++r) l[r] *= bc[32 + r];
+        for (int r = 0; r < H; ++r) l[r] = l[r] * bc[32 + r] * bc[32 + r];
       }
 #pragma unroll
       for (int r = 0; r < H; r += 2) {
@@ -331,6 +339,9 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
       }
       if (rare(!first && moved)) {
         tc_fence_after_sync();
+        __syncwarp();
+        if (lane < H) bc[32 + lane] = root * root * power_of_two(-shift);
+        __syncwarp();
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
           uint32_t o[H];

@@ -82,8 +82,8 @@ constexpr int kOffP = kOffQ + kQBytes;
 constexpr int kOffScale = kOffP + 2 * kPBytes;
 constexpr int kOffMx = kOffScale + kScaleSlots * kTile * 4;  // float[2][kSlices][64] partial maxima, and row sums
 constexpr int kOffUnit = kOffMx + 2 * kSlices * kRows * 4;             // float[kScaleSlots][3][128] scales; their part in the weights; its log2
-constexpr int kOffBound = kOffUnit + 3 * kScaleSlots * kTile * 4;  // float[kScaleSlots][2] R, whether a scale is 0 or not finite
-constexpr int kOffC = kOffBound + kScaleSlots * 8;           // float[kCSlots][64] c_r of the last segments
+constexpr int kOffBound = kOffUnit + 3 * kScaleSlots * kTile * 4;  // float[kScaleSlots][4] R, whether a scale is 0 or not finite, log2 of R's move
+constexpr int kOffC = kOffBound + kScaleSlots * 16;          // float[kCSlots][64] c_r of the last segments
 constexpr int kOffRow = kOffC + kCSlots * kRows * 4;         // int[64] row in the sequence
 constexpr int kOffBar = kOffRow + kRows * 4;
 // Barriers, in each CTA.  The kPeer ones are CTA 0's view of CTA 1, whose warps
@@ -290,7 +290,7 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
       const uint32_t s_at = tmem + lanes + kTmemS + (n & 1) * 128 + g * 16;
       const float* const raw = scales + (n & 3) * kTile + page * kPage + g * 16;
       const float* const factors = factors_of + (n & 3) * (3 * kTile) + page * kPage + g * 16;
-      const float* const bnd = bounds + 2 * (n & 3);
+      const float* const bnd = bounds + 4 * (n & 3);
       if (rare(ragged || bnd[1] != 0.f)) {
         // Before they are read below, scores of hidden tokens become -inf, those of tokens
         // whose scale is not finite NaN, and those of scale 0 zero: the factor of the last
@@ -364,13 +364,18 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
       m = mxb[row];
 #pragma unroll
       for (int k = 1; k < kSlices; ++k) m = fmaxf(m, mxb[k * kRows + row]);
-      float alpha = 1.f;
-      if (m > m_run + kSlack) {
-        if (!first) m += kMargin;
-        alpha = ex2_approx(m_run - m);  // 0 from -inf
-        m_run = m;
-        neg = -m;
+      float root = 1.f, alpha = 1.f;  // l moves by root^2, O by alpha
+      float to = m_run;
+      const float shift = bnd[2];
+      if (rare(shift != 0.f) && m != -INFINITY) to -= fminf(shift, kMaxLess);
+      if (m > to + kSlack) to = first ? m : m + kMargin;
+      if (to != m_run) {
+        root = root_of_move(m_run - to);  // 0 from -inf
+        alpha = root * root;
+        m_run = to;
+        neg = -to;
       }
+      if (rare(shift != 0.f)) alpha *= power_of_two(-static_cast<int>(shift));
       const bool moved = __any_sync(0xffffffffu, alpha != 1.f);
 
       // ---- weights as hi and lo bytes, a 16-byte unit of P's row, and their sum
@@ -411,7 +416,7 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
         f2_split(f2_add(l2[0], l2[1]), a, b);
         sum = a + b;
       }
-      l_run = l_run * alpha + sum;
+      l_run = l_run * root * root + sum;
 
       if (rare(ragged)) {
         // where a hidden entry may hold anything, NaN codes of V become 0 (a zero
@@ -560,18 +565,23 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
         const float4 s4 = reinterpret_cast<const float4*>(gbase + kOffScale)[(m & 3) * 32 + lane];
         float s[4] = {s4.x, s4.y, s4.z, s4.w}, scale[4];
         bool odd = false;
-        uint32_t top = 0;
+        uint32_t top = 0, any = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const bool fine = s[e] > 0.f && s[e] < INFINITY;
           odd = odd || (e < end && !fine);
           scale[e] = e < end && fine ? s[e] : 1.f;
           if (!(e < end && fine)) s[e] = 0.f;
+          any = max(any, __float_as_uint(s[e]));
           if (e < all_see || 4 * lane + e == 0) top = max(top, __float_as_uint(s[e]));
         }
         odd = __any_sync(0xffffffffu, odd);
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (next.first()) bound = fminf(fmaxf(__uint_as_float(top), kMinR), kMaxR);
+        float shift = 0.f;
+        if (rare(next.first() || bound == kMinR)) {
+          const float r = reference_scale(__reduce_max_sync(0xffffffffu, top), __reduce_max_sync(0xffffffffu, any));
+          if (!next.first()) shift = static_cast<float>(log2_of_power(r) - log2_of_power(bound));
+          bound = r;
+        }
         const float u = 1.f / bound;
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[e] = fminf(s[e] * u, kMaxRatio);
@@ -580,8 +590,9 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
         to[32] = make_float4(s[0] * kUnit, s[1] * kUnit, s[2] * kUnit, s[3] * kUnit);
         to[64] = make_float4(log_ratio(s[0]), log_ratio(s[1]), log_ratio(s[2]), log_ratio(s[3]));
         if (lane == 0) {
-          bounds[2 * (m & 3)] = bound;
-          bounds[2 * (m & 3) + 1] = odd ? 1.f : 0.f;
+          bounds[4 * (m & 3)] = bound;
+          bounds[4 * (m & 3) + 1] = odd ? 1.f : 0.f;
+          bounds[4 * (m & 3) + 2] = shift;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kUnitFull + (m & 3)));

@@ -18,11 +18,12 @@ constexpr int kTile = 128;  // tokens: two pages
 // is near kUnit whatever the scales beside it are, those of tokens that it does not
 // see among them.  M is moved (and O rescaled, between two products) only when it
 // grew by more than kSlack (log2): weights stay below kUnit 2^kSlack < 448, e4m3's
-// largest.  R, the largest scale of the segment's first tile over the tokens that every
-// row sees and the first one, serves the range only: P and its sum l reach R / scale.
+// largest.  R, a power of two, serves the range only: P and its sum l reach R / scale.
+// It is made from the segment's first tile, or, while there is nothing above kMinR, from
+// the first one that holds more (see move_reference).
 constexpr float kMargin = 1.f;             // a maximum that moves goes this far beyond, so that it moves less often
-constexpr float kMinR = 0x1p-60f, kMaxR = 0x1p120f;
-constexpr float kMaxRatio = 0x1p100f;      // of scale / R
+constexpr float kMinR = 0x1p-60f, kMaxR = 0x1p40f;
+constexpr float kMaxRatio = 0x1p101f;      // of scale / R
 constexpr float kMinLog = -80.f;           // of its log2, as far as M goes; 0 has it too
 
 __device__ __forceinline__ float log_ratio(float ratio) {
@@ -30,6 +31,28 @@ __device__ __forceinline__ float log_ratio(float ratio) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(ratio));
   return fmaxf(y, kMinLog);
 }
+
+__device__ __forceinline__ int log2_of_power(float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; }  // positive, normal
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // normal ones
+
+// R of a tile, from the bits of its largest finite scales: `top` over the tokens that every
+// row sees and the first one, which every row that sees one of the segment's sees; `any` over
+// all inside the sequence, some of which only some rows see.  Those count only where the
+// others have next to nothing, and as little as keeps them below kMaxRatio.
+__device__ __forceinline__ float reference_scale(uint32_t top, uint32_t any) {
+  float r = __uint_as_float(top & 0x7f800000u);  // the power of two at or below it
+  if (!(r > kMinR)) r = fmaxf(kMinR, __uint_as_float(any & 0x7f800000u) * 0x1p-100f);
+  return fminf(r, kMaxR);
+}
+
+// Where R moves from kMinR to a later tile's, what the rows have so far is of tokens of next
+// to no scale.  Their P and l do not change, O, in units of R, does, and M, in terms of
+// scale / R, may come down by as much: by kMaxLess at most, for l <= tokens * 2^80 grows by that.
+constexpr float kMaxLess = 24.f;
+
+// A move of M by d changes l by 2^d, which is made as the square of this: l may reach 2^80
+// by tokens of no scale, and what is then left of it still counts although 2^d is below 2^-126.
+__device__ __forceinline__ float root_of_move(float d) { return ex2_approx(0.5f * d); }
 
 // m + log2(l) where both may be large and of opposite signs.
 __device__ __forceinline__ float log_sum(float m, float l) {

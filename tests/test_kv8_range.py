@@ -63,3 +63,28 @@ def test_few_tokens_at_the_far_end_of_the_range(h_q, s_q):
         ref = attention(*x, SCALE, True)
         for parts in (None, 1, 4, 60):
             held(*decode(*x, causal=True, parts=parts), ref)
+
+
+@gpu
+@pytest.mark.parametrize("h_q,s_q", [(16, 1), (40, 1), (128, 1), (20, 3), (96, 2)])
+@pytest.mark.parametrize("kind", ["scale 0", "written zeros", "scale 2^-70"])
+def test_first_tokens_of_next_to_nothing(h_q, s_q, kind):
+    """Tokens whose entries are zero or next to it count in the softmax like any others, and those after them too, whatever
+    their scales."""
+    lens = [256, 300, 700, 1000, 129, 128, 5]
+    gone = 190
+    q0, cache, scales0, bt, sl = inputs(lens, s_q, h_q, seed=52)
+    codes = cache.view(torch.uint8)
+    for i, L in enumerate(lens):
+        for t in range(min(L, gone)):
+            scales0[at(bt, i, t)] = {"scale 0": 0.0, "written zeros": 2.0 ** -126, "scale 2^-70": 2.0 ** -70}[kind]
+            if kind == "written zeros":
+                codes[int(bt[i, t // 64]), t % 64] = 0
+    for power in (0, 4, 20, 46, 60, 100):
+        scales = torch.where(scales0 > 2.0 ** -60, scales0 * 2.0 ** power, scales0)
+        for level in (1.0, 6.0):  # of the scores
+            q = (q0.float() * (level * 2.0 ** -power)).to(torch.bfloat16)
+            x = (q, cache, scales, bt, sl)
+            ref = attention(*x, SCALE, s_q > 1)
+            for parts in (None, 1, 5):
+                held(*decode(*x, causal=s_q > 1, parts=parts), ref)
