@@ -75,7 +75,11 @@ bool rows_apart(const Rows& a, const Rows& b, int64_t tokens, int64_t dim, int64
   return gap >= dim && gap <= inner - dim;
 }
 
-mla_status_t done(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
+mla_status_t done(cudaError_t e) {
+  if (e == cudaSuccess) return MLA_OK;
+  cudaGetLastError();  // a launch that failed is this call's to report, not the next one's
+  return MLA_ERR_CUDA;
+}
 
 }  // namespace
 
@@ -175,7 +179,8 @@ mla_status_t mla_decode_kv8(const void* q, int b, int s_q, int h_q, int d, const
   p.max_blocks = max_blocks_per_seq;
   p.causal = causal;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
-  if (mla::launch_decode_kv8(p, num_parts, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
+  r = done(mla::launch_decode_kv8(p, num_parts, reinterpret_cast<cudaStream_t>(stream)));
+  if (r != MLA_OK) return r;
   mla::CombineParams m;
   m.num_splits = num_splits;
   m.ws_o = p.ws_o;

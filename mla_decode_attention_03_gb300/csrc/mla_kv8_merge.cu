@@ -116,8 +116,10 @@ cudaError_t launch_merge_kv8(const CombineParams& p, cudaStream_t stream) {
   // Where a sequence has many pieces a row's four warps keep them all in flight, with
   // one or two a warp does: 16 sequences over 152 parts 15.4 us a call with four warps,
   // 19.5 with one; 37 over 76 25.3 and 25.8; 128 over 76 130.7 and 125.0.
-  const bool many = p.num_parts >= 2 * p.b;
-  const int rows = p.s_q * p.h_q, each = many ? 1 : 4;
+  // (A grid's second dimension ends at 65535, the rows that a call may have at four times that.)
+  const int rows = p.s_q * p.h_q;
+  const bool many = p.num_parts >= 2 * static_cast<int64_t>(p.b) && rows <= 65535;
+  const int each = many ? 1 : 4;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.b, (rows + each - 1) / each, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);

@@ -88,3 +88,14 @@ def test_first_tokens_of_next_to_nothing(h_q, s_q, kind):
             ref = attention(*x, SCALE, s_q > 1)
             for parts in (None, 1, 5):
                 held(*decode(*x, causal=s_q > 1, parts=parts), ref)
+
+
+@gpu
+@pytest.mark.parametrize("h_q,s_q", [(128, 512), (4, 16384)])
+def test_more_rows_than_a_grid_dimension(h_q, s_q):
+    """65536 rows a sequence, in two pieces: the merge takes them."""
+    x = inputs([200], s_q, h_q, seed=57)
+    out, lse = decode(*x, parts=2, causal=False)
+    some = [0, 1, s_q // 2, s_q - 1]
+    ref = attention(x[0][:, some], *x[1:], SCALE, False)
+    held(out[:, some], lse[..., some], ref)
