@@ -99,3 +99,22 @@ def test_more_rows_than_a_grid_dimension(h_q, s_q):
     some = [0, 1, s_q // 2, s_q - 1]
     ref = attention(x[0][:, some], *x[1:], SCALE, False)
     held(out[:, some], lse[..., some], ref)
+
+
+@gpu
+@pytest.mark.parametrize("h_q", [16, 64, 128])
+def test_infinite_scale_makes_a_row_nan(h_q):
+    lens = [64, 700, 129]
+    q, cache, scales, bt, sl = inputs(lens, 2, h_q, seed=56)
+    for parts in (1, 9):
+        first = decode(q, cache, scales, bt, sl, causal=True, parts=parts)
+        for t_of in (lambda L: L - 1, lambda L: 0):
+            bad = scales.clone()
+            for i, L in enumerate(lens):
+                bad[at(bt, i, t_of(L))] = math.inf
+            out, lse = decode(q, cache, bad, bt, sl, causal=True, parts=parts)
+            assert torch.isnan(out[:, 1]).all() and torch.isnan(lse[..., 1]).all()
+            if t_of(64):
+                assert torch.equal(out[:, 0], first[0][:, 0]) and torch.equal(lse[..., 0], first[1][..., 0])
+            else:
+                assert torch.isnan(out).all() and torch.isnan(lse).all()
