@@ -9,7 +9,9 @@ the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
+from fractions import Fraction
 from pathlib import Path
 
 import torch
@@ -630,6 +632,28 @@ class MLADecoderFP8:
 _ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # MLA_BF16, MLA_FP16, MLA_FP32
 
 
+_PI_BITS = 1300  # 64 below a turn of the largest double, 2^1024, with some to spare
+
+
+@functools.lru_cache(None)
+def _pi() -> int:
+    """pi * 2^_PI_BITS, by pi = 16 arctan(1/5) - 4 arctan(1/239)."""
+    def arctan_of_inverse(x):
+        term = (1 << (_PI_BITS + 32)) // x
+        total, n = term, 1
+        while term:
+            term //= -x * x
+            n += 2
+            total += term // n
+        return total
+    return (16 * arctan_of_inverse(5) - 4 * arctan_of_inverse(239)) >> 32
+
+
+def _turns(f: float) -> int:
+    """f radians as turns in 64-bit fixed point, whole turns dropped, rounded once."""
+    return round(Fraction(f) * (1 << (_PI_BITS + 63)) / _pi()) % (1 << 64)
+
+
 class Rotary:
     """A model's rotary frequencies, on the device, for rope().
 
@@ -662,7 +686,7 @@ class Rotary:
                     freq[i] = freq[i] / factor * ramp + freq[i] * (1.0 - ramp)
         self.dim, self.interleaved, self.gain, self.frequencies = dim, int(bool(interleaved)), float(gain), freq
         # turns per position in 64-bit fixed point (two's complement in an int64 tensor)
-        turns = [round(f / (2 * math.pi) * 2.0 ** 64) % (1 << 64) for f in freq]
+        turns = [_turns(f) for f in freq]
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.turns = torch.tensor([t - (1 << 64) if t >= 1 << 63 else t for t in turns], dtype=torch.int64, device=device)
 
