@@ -741,7 +741,8 @@ def rope(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, out: torch.Te
         raise MLAError("k_out without k")
     else:
         ks = (None, 0, 0, None, 0, 0, 0)
-    if n > 0 and xs[6] > 0:
-        _call("mla_rope", load_library().mla_rope, dev, *xs, *ks, n, dim, positions.data_ptr(), width, rotary.turns.data_ptr(),
-              rotary.gain, rotary.interleaved, 1 if inverse else 0, dtype)
+    first, second = (xs, ks) if xs[6] > 0 else (ks, (None, 0, 0, None, 0, 0, 0))  # x may have no heads
+    if n > 0 and first[6] > 0:
+        _call("mla_rope", load_library().mla_rope, dev, *first, *second, n, dim, positions.data_ptr(), width,
+              rotary.turns.data_ptr(), rotary.gain, rotary.interleaved, 1 if inverse else 0, dtype)
     return out if k is None else (out, k_out)
