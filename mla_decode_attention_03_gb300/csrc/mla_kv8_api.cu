@@ -75,6 +75,9 @@ bool rows_apart(const Rows& a, const Rows& b, int64_t tokens, int64_t dim, int64
   return gap >= dim && gap <= inner - dim;
 }
 
+// Rows of a sequence that a decode takes (see check_decode_args); s_q (h_q / h_kv) is an int below.
+bool too_many_rows(int s_q, int h_q) { return static_cast<int64_t>(s_q) * h_q > 4 * 65535; }
+
 mla_status_t done(cudaError_t e) {
   if (e == cudaSuccess) return MLA_OK;
   cudaGetLastError();  // a launch that failed is this call's to report, not the next one's
@@ -118,7 +121,7 @@ mla_status_t mla_read_cache_kv8(const void* codes, const float* scales, int64_t 
 
 int mla_num_parts_kv8(int s_q, int h_q, int h_kv, int device) {
   if (s_q < 1 || h_q < 1 || h_kv < 1 || h_q % h_kv != 0) return MLA_ERR_INVALID_ARG;
-  if (h_q / h_kv > mla::kRowsPerTile) return MLA_ERR_UNSUPPORTED;
+  if (h_q / h_kv > mla::kRowsPerTile || too_many_rows(s_q, h_q)) return MLA_ERR_UNSUPPORTED;
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
     cudaGetLastError();
@@ -131,7 +134,7 @@ int mla_num_parts_kv8(int s_q, int h_q, int h_kv, int device) {
 
 size_t mla_workspace_bytes_kv8(int b, int s_q, int h_q, int h_kv, int num_parts) {
   const size_t parts = mla_workspace_bytes(b, s_q, h_q, num_parts);
-  if (parts == 0 || h_kv < 1 || h_q % h_kv != 0) return 0;
+  if (parts == 0 || h_kv < 1 || h_q % h_kv != 0 || too_many_rows(s_q, h_q)) return 0;
   return parts + mla::decode_kv8_query_bytes(b, h_kv, s_q * (h_q / h_kv));
 }
 
