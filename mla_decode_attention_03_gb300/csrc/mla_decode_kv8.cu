@@ -223,7 +223,7 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
       }
       // (a NaN scale counts as 0 here: to a row that does not see it, it is nothing)
       const float ratio = scale < INFINITY ? fminf(scale * (1.f / bound), kMaxRatio) : 0.f;
-      const float log_of = log_ratio(ratio);
+      const float log_of = log_ratio(ratio), factor = scale * kFactorUnit;
 
       // ---- scores
       ok = warp_wait(bar(C::SFull + (n & 1)), (n >> 1) & 1, abort_flag);
@@ -242,7 +242,7 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::SEmpty + (n & 1)));
 #pragma unroll
-        for (int r = 0; r < H; ++r) v[r] = (__uint_as_float(hi[r]) + __uint_as_float(lo[r])) * scale * c_row[r];
+        for (int r = 0; r < H; ++r) v[r] = (__uint_as_float(hi[r]) + __uint_as_float(lo[r])) * factor * c_row[r];
       }
       if (rare(ragged)) {
 #pragma unroll

@@ -551,7 +551,7 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
       next = w;
       int n = 0, m = 0;
       float bound = 1.f;
-      // The scales (1 past the end, and for one that is 0 or not finite), kUnit scale / R (0 there), and
+      // The scales, times kFactorUnit (1 past the end, and for one that is 0 or not finite), kUnit scale / R (0 there), and
       // log2(scale / R).  R is over the tokens that every row sees, and the first, which every row that sees one
       // of the segment's tokens sees.  A row that sees a token whose scale is not finite gets a NaN score; to the
       // others it is nothing.  Four slots: factors m + 4 are made once S(m + 3) is
@@ -570,7 +570,7 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
         for (int e = 0; e < 4; ++e) {
           const bool fine = s[e] > 0.f && s[e] < INFINITY;
           odd = odd || (e < end && !fine);
-          scale[e] = e < end && fine ? s[e] : 1.f;
+          scale[e] = e < end && fine ? fmaxf(s[e] * kFactorUnit, 0x1p-149f) : 1.f;
           if (!(e < end && fine)) s[e] = 0.f;
           any = max(any, __float_as_uint(s[e]));
           if (e < all_see || 4 * lane + e == 0) top = max(top, __float_as_uint(s[e]));

@@ -181,7 +181,7 @@ mla_status_t mla_decode_kv8(const void* q, int b, int s_q, int h_q, int d, const
   p.rows = s_q * p.heads_per_kv;
   p.max_blocks = max_blocks_per_seq;
   p.causal = causal;
-  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f * (1.f / mla::kFactorUnit);
   r = done(mla::launch_decode_kv8(p, num_parts, reinterpret_cast<cudaStream_t>(stream)));
   if (r != MLA_OK) return r;
   mla::CombineParams m;

@@ -9,6 +9,10 @@
 
 namespace mla {
 
+// A score is (product x scale kFactorUnit) x c, with 1 / kFactorUnit in c: a product of a row's and
+// a token's codes is up to 2^27, a scale up to 2^120, and a query may be as small as the scale is large.
+constexpr float kFactorUnit = 0x1p-7f;
+
 struct DecodeKv8Params {
   const void* q;                 // bf16 [b, s_q, h_q, 576]
   const uint8_t* codes;          // e4m3 entries
@@ -31,7 +35,7 @@ struct DecodeKv8Params {
   int rows;                      // s_q * heads_per_kv: query rows per KV head
   int max_blocks;
   int causal;
-  float scale_log2;              // softmax_scale * log2(e)
+  float scale_log2;              // softmax_scale * log2(e) / kFactorUnit
 };
 
 bool decode_kv8_in_pairs(int rows);

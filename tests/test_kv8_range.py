@@ -118,3 +118,14 @@ def test_infinite_scale_makes_a_row_nan(h_q):
                 assert torch.equal(out[:, 0], first[0][:, 0]) and torch.equal(lse[..., 0], first[1][..., 0])
             else:
                 assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+
+@gpu
+@pytest.mark.parametrize("h_q", [16, 40, 128])
+@pytest.mark.parametrize("power", [-112, 118])
+def test_scores_of_large_and_small_factors(h_q, power):
+    """Entries near the ends of bf16's range and queries at the other end: the scores are ordinary."""
+    q, cache, scales, bt, sl = inputs([300, 70, 1], 1, h_q, seed=55)
+    x = ((q.float() * 2.0 ** -power).to(torch.bfloat16), cache, scales * 2.0 ** power, bt, sl)
+    held(*decode(*x), attention(*x, SCALE, False))
