@@ -389,7 +389,7 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
         if (rare(!ok)) break;
         if (lane < H) {
           const float t = (ls[lane] + ls[32 + lane]) + (ls[64 + lane] + ls[96 + lane]);
-          bc[lane] = t == 0.f ? 0.f : bound / (kUnit * t);
+          bc[lane] = t == 0.f ? 0.f : 1.f / (kUnit * t);  // and R apart: the two may be far below 2^-126 together
           const int row = row_of[g * H + lane];
           if (quad == 0 && row >= 0) {
             const float lse = t == 0.f ? -INFINITY : log_sum(m_run, t) * 0.69314718055994531f;
@@ -416,14 +416,14 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
           hold(o);
           hold(lo);
 #pragma unroll
-          for (int r = 0; r < H; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) + __uint_as_float(lo[r]));
+          for (int r = 0; r < H; ++r) o[r] = __float_as_uint((__uint_as_float(o[r]) + __uint_as_float(lo[r])) * bc[r] * bound);
           const int dim = c * 128 + tl;
           if (whole) {
             // two rows at a time: even lanes store a pair of dims of the first, odd lanes of the second
             __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(P.out) + out_row * kDimV + (dim & ~1);
 #pragma unroll
             for (int r = 0; r < H; r += 2) {
-              const float a = __uint_as_float(o[r]) * bc[r], b = __uint_as_float(o[r + 1]) * bc[r + 1];
+              const float a = __uint_as_float(o[r]), b = __uint_as_float(o[r + 1]);
               const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
               const int row = row_of[g * H + r + (lane & 1)];
               if (row >= 0)
@@ -435,7 +435,7 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
 #pragma unroll
             for (int r = 0; r < H; ++r) {
               const int row = row_of[g * H + r];
-              if (row >= 0) dst[static_cast<int64_t>(row) * kDimV] = __uint_as_float(o[r]) * bc[r];
+              if (row >= 0) dst[static_cast<int64_t>(row) * kDimV] = __uint_as_float(o[r]);
             }
           }
         }

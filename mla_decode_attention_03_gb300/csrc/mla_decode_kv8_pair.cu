@@ -479,7 +479,7 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
         float t = 0.f;
 #pragma unroll
         for (int k = 0; k < kSlices; ++k) t += mxb[k * kRows + row];
-        const float inv = t == 0.f ? 0.f : bnd[0] / (kUnit * t);
+        const float inv = t == 0.f ? 0.f : 1.f / (kUnit * t), bound = bnd[0];  // the two may be far below 2^-126 together
         const int my_row = row_of[row];
         if (slice == 0 && my_row >= 0) {
           const float lse = t == 0.f ? -INFINITY : log_sum(m_run, t) * 0.69314718055994531f;
@@ -511,7 +511,7 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
             uint32_t b[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              b[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+              b[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv * bound, __uint_as_float(o[2 * e + 1]) * inv * bound);
             turn_4x4x16(b, lane);
             __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(P.out) + out_row * kDimV + dim + (lane & 3) * 8;
 #pragma unroll
@@ -521,7 +521,7 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
                     make_uint4(b[4 * j], b[4 * j + 1], b[4 * j + 2], b[4 * j + 3]);
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv * bound);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t* const q = o + 16 * h;

@@ -120,7 +120,6 @@ def test_infinite_scale_makes_a_row_nan(h_q):
                 assert torch.isnan(out).all() and torch.isnan(lse).all()
 
 
-
 @gpu
 @pytest.mark.parametrize("h_q", [16, 40, 128])
 @pytest.mark.parametrize("power", [-112, 118])
@@ -129,3 +128,17 @@ def test_scores_of_large_and_small_factors(h_q, power):
     q, cache, scales, bt, sl = inputs([300, 70, 1], 1, h_q, seed=55)
     x = ((q.float() * 2.0 ** -power).to(torch.bfloat16), cache, scales * 2.0 ** power, bt, sl)
     held(*decode(*x), attention(*x, SCALE, False))
+
+
+@gpu
+@pytest.mark.parametrize("h_q", [16, 40, 128])
+def test_smallest_entries_keep_their_bits(h_q):
+    """Entries of the smallest scale, 2^-126: the outputs are held relative to themselves, down to bf16's smallest step."""
+    q, cache, scales, bt, sl = inputs([700, 3, 20000], 1, h_q, seed=54)
+    scales.fill_(2.0 ** -126)
+    cache.view(torch.uint8)[..., :512] &= 0x7F  # of one sign, so that the outputs are as large as their parts
+    x = (q, cache, scales, bt, sl)
+    o, l, ob, lb = attention(*x, SCALE, False)
+    for parts in (None, 1):
+        out, lse = decode(*x, parts=parts)
+        held(out, lse, (o, l, ob - 1e-30 + 2.0 ** -133, lb))
