@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import threading
 from fractions import Fraction
 from pathlib import Path
 
@@ -113,10 +114,41 @@ def new_status(device=None) -> torch.Tensor:
     return torch.zeros(1, dtype=torch.int32, device=device or torch.cuda.current_device())
 
 
-def check_status(status: torch.Tensor):
-    """Synchronises on the status word and raises if a kernel reported an error."""
+_shared_status: dict[int, torch.Tensor] = {}
+_shared_status_lock = threading.Lock()
+
+
+def _status_of_device(device: torch.device) -> torch.Tensor:
+    """The word that calls on the 8-bit cache without one of their own report to: made once per device, so that they
+    neither allocate nor fill.  (A first call inside a stream capture gets a word of the capture's own.)"""
+    word = _shared_status.get(device.index)
+    if word is None:
+        with torch.cuda.device(device):
+            if torch.cuda.is_current_stream_capturing():
+                return new_status(device)
+            with _shared_status_lock:
+                word = _shared_status.get(device.index)
+                if word is None:
+                    word = new_status(device)
+                    torch.cuda.current_stream().synchronize()  # zero before any stream's kernel may report
+                    _shared_status[device.index] = word
+    return word
+
+
+def check_status(status: torch.Tensor | None = None):
+    """Synchronises on the status word and raises if a kernel reported an error.  Without a word: waits for the current
+    device and looks at what the calls on the 8-bit cache that were given none reported there, clearing it."""
+    shared = status is None
+    if shared:
+        status = _shared_status.get(torch.cuda.current_device())
+        if status is None:
+            return
+        torch.cuda.synchronize(status.device)
     code = int(status.item())
     if code != 0:
+        if shared:
+            status.zero_()
+            torch.cuda.current_stream(status.device).synchronize()
         raise MLAError(f"device reported {status_string(code)} ({code})")
 
 
@@ -456,7 +488,7 @@ def _check_cache_fp8(kcache, scales):
 
 def _status_word(status, device):
     if status is None:
-        return new_status(device)
+        return _status_of_device(device) if device.type == "cuda" else new_status(device)  # (refused by who asked)
     if status.dtype is not torch.int32 or status.device != device or status.numel() < 1:
         raise MLAError(f"status must be an int32 word on {device}")
     return status
@@ -465,7 +497,8 @@ def _status_word(status, device):
 def write_cache_fp8(kv_c: torch.Tensor, k_pe: torch.Tensor, slot_mapping: torch.Tensor, kcache: torch.Tensor,
                     scales: torch.Tensor, status: torch.Tensor | None = None):
     """New tokens into the 8-bit cache (mla_write_cache_kv8): entry slot_mapping[t] <- [kv_c[t], k_pe[t]] as e4m3 with one
-    power-of-two scale.  Slots below 0 are skipped; the others must differ from one another."""
+    power-of-two scale.  Slots below 0 are skipped; the others must differ from one another.  What the device finds wrong
+    goes to `status`, or without one to the device's word that check_status() looks at."""
     nb, h_kv, stride = _check_cache_fp8(kcache, scales)
     if h_kv != 1:
         raise MLAError("MLA caches have one latent head")
@@ -498,7 +531,7 @@ def read_cache_fp8(kcache: torch.Tensor, scales: torch.Tensor, block_table: torc
                    status: torch.Tensor | None = None):
     """Entries of ragged token ranges back as bf16 rows (mla_read_cache_kv8): row cu_tokens[i] + n is token
     starts[i] + n (starts: 0 where None) of sequence i.  Returns out [total, 576]; a given `out` may have more rows.
-    Rows from cu_tokens[-1] on are left as they were."""
+    Rows from cu_tokens[-1] on are left as they were.  `status` as for write_cache_fp8."""
     nb, h_kv, stride = _check_cache_fp8(kcache, scales)
     if h_kv != 1:
         raise MLAError("MLA caches have one latent head")
@@ -548,7 +581,8 @@ def mla_decode_fp8(q: torch.Tensor, kcache: torch.Tensor, scales: torch.Tensor, 
                    softmax_scale: float, causal: bool = False, out: torch.Tensor | None = None,
                    lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                    status: torch.Tensor | None = None):
-    """MLA decode over the 8-bit cache (mla_decode_kv8): returns (out bf16[b, s_q, h_q, 512], lse fp32[b, h_q, s_q])."""
+    """MLA decode over the 8-bit cache (mla_decode_kv8): returns (out bf16[b, s_q, h_q, 512], lse fp32[b, h_q, s_q]).
+    `status` as for write_cache_fp8."""
     if q.dim() != 4:
         raise MLAError(f"q must be [b, s_q, h_q, 576], got {tuple(q.shape)}")
     b, s_q, h_q, _ = q.shape
