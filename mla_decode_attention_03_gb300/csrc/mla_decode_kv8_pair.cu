@@ -861,11 +861,13 @@ cudaError_t configure() {
 
 }  // namespace
 
-size_t decode_kv8_query_bytes(int b, int h_kv, int rows) {
-  if (!decode_kv8_in_pairs(rows)) return 0;
-  const size_t tiles = static_cast<size_t>(b) * h_kv * (2 * ((rows + 2 * kRows - 1) / (2 * kRows)));
-  return tiles * (kQBytes + kRows * 4);
+static size_t query_tiles(int b, int h_kv, int rows) {
+  return decode_kv8_in_pairs(rows) ? static_cast<size_t>(b) * h_kv * (2 * ((rows + 2 * kRows - 1) / (2 * kRows))) : 0;
 }
+
+size_t decode_kv8_factors_at(int b, int h_kv, int rows) { return query_tiles(b, h_kv, rows) * kQBytes; }
+
+size_t decode_kv8_query_bytes(int b, int h_kv, int rows) { return query_tiles(b, h_kv, rows) * (kQBytes + kRows * 4); }
 
 cudaError_t launch_decode_kv8_pair(const DecodeKv8Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int num_parts,
                                    cudaStream_t stream) {

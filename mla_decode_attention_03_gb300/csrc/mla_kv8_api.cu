@@ -169,7 +169,7 @@ mla_status_t mla_decode_kv8(const void* q, int b, int s_q, int h_q, int d, const
   p.ws_o = static_cast<float*>(workspace);
   p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + o_bytes);
   p.ws_q = static_cast<uint8_t*>(workspace) + mla_workspace_bytes(b, s_q, h_q, num_parts);
-  p.ws_c = reinterpret_cast<float*>(p.ws_q + mla::decode_kv8_query_bytes(b, h_kv, s_q * (h_q / h_kv)) / (73728 + 256) * 73728);
+  p.ws_c = reinterpret_cast<float*>(p.ws_q + mla::decode_kv8_factors_at(b, h_kv, s_q * (h_q / h_kv)));
   p.status = status;
   p.num_blocks = num_blocks;
   p.entry_bytes = stride;

@@ -40,7 +40,8 @@ struct DecodeKv8Params {
 
 bool decode_kv8_in_pairs(int rows);
 int decode_kv8_ctas(int rows);  // CTAs per part and KV head
-size_t decode_kv8_query_bytes(int b, int h_kv, int rows);
+size_t decode_kv8_query_bytes(int b, int h_kv, int rows);    // codes, then factors
+size_t decode_kv8_factors_at(int b, int h_kv, int rows);     // offset of the factors
 cudaError_t launch_decode_kv8_pair(const DecodeKv8Params& p, const CUtensorMap& lat, const CUtensorMap& rope, int num_parts,
                                    cudaStream_t stream);
 cudaError_t launch_decode_kv8(const DecodeKv8Params& p, int num_parts, cudaStream_t stream);
