@@ -85,7 +85,10 @@ mla_status_t mla_read_cache_kv8(const void *codes, const float *scales, int64_t 
  * An entry that a query does see and that holds a NaN, or whose scale is not
  * finite, makes its row NaN.  A weight p_t scale_t is held to 2^-8 of itself (2^-7
  * for more than 64 query rows per KV head) or 2^-16 of its row's largest, as long as
- * the scales of a sequence lie within 2^80 of one another.  For more than 262140
+ * the scales of a sequence that are above 2^-60 lie within 2^80 of one another (smaller
+ * ones beside them, those of zero entries among them, count in full in the softmax);
+ * where all that every query sees is at or below 2^-60, what only some see may be up to
+ * 2^75.  For more than 262140
  * rows s_q h_q, which no decode takes, the two sizes are MLA_ERR_UNSUPPORTED and 0.
  */
 int mla_num_parts_kv8(int s_q, int h_q, int h_kv, int device);

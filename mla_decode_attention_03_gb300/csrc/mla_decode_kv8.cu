@@ -180,6 +180,7 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
     float l[H];
     float m_run = -INFINITY;   // of row g H + lane (lanes below H)
     float bound = 1.f;         // R
+    bool nothing = false;      // of which R was made
     int L = 0, seg_end = 0, all_see = 0;
     const float* c_row = nullptr;
 
@@ -208,16 +209,16 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
       float scale = tok < seg_end ? sc[tl] : 0.f;
       if (!(scale < INFINITY)) scale = __uint_as_float(0x7fffffffu);  // a row that sees it becomes NaN
       int shift = 0;                                       // by which log2(R) moves
-      if (rare(first || bound == kMinR)) {
-        uint32_t top = 0, any = 0;
+      if (rare(first || (nothing && t0 < all_see))) {
+        uint32_t top = 0;
 #pragma unroll 1
         for (int e = lane; e < kTile; e += 32) {
           const uint32_t a = __float_as_uint(sc[e]);
-          if (t0 + e >= seg_end || a >= 0x7f800000u) continue;
-          any = max(any, a);
-          if (t0 + e < all_see || e == 0) top = max(top, a);
+          if ((t0 + e < all_see || (first && e == 0)) && a < 0x7f800000u) top = max(top, a);
         }
-        const float r = reference_scale(__reduce_max_sync(0xffffffffu, top), __reduce_max_sync(0xffffffffu, any));
+        top = __reduce_max_sync(0xffffffffu, top);
+        nothing = is_nothing(top);
+        const float r = reference_scale(top);
         if (!first) shift = log2_of_power(r) - log2_of_power(bound);
         bound = r;
       }
@@ -268,9 +269,7 @@ mla_decode_kv8_kernel(const __grid_constant__ CUtensorMap lat_map, const __grid_
       float root = 1.f;  // of the factor by which l moves
       if (lane < H) {
         const float m = fmaxf(fmaxf(mxb[lane], mxb[32 + lane]), fmaxf(mxb[64 + lane], mxb[96 + lane]));
-        float to = m_run;
-        if (rare(shift != 0) && m != -INFINITY) to -= fminf(static_cast<float>(shift), kMaxLess);
-        if (m > to + kSlack) to = m;
+        const float to = m > m_run + kSlack ? m : m_run;
         if (to != m_run) {
           root = root_of_move(m_run - to);  // 0 from -inf
           m_run = to;

@@ -365,17 +365,14 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
 #pragma unroll
       for (int k = 1; k < kSlices; ++k) m = fmaxf(m, mxb[k * kRows + row]);
       float root = 1.f, alpha = 1.f;  // l moves by root^2, O by alpha
-      float to = m_run;
-      const float shift = bnd[2];
-      if (rare(shift != 0.f) && m != -INFINITY) to -= fminf(shift, kMaxLess);
-      if (m > to + kSlack) to = first ? m : m + kMargin;
+      const float to = m > m_run + kSlack ? (first ? m : m + kMargin) : m_run;
       if (to != m_run) {
         root = root_of_move(m_run - to);  // 0 from -inf
         alpha = root * root;
         m_run = to;
         neg = -to;
       }
-      if (rare(shift != 0.f)) alpha *= power_of_two(-static_cast<int>(shift));
+      if (rare(bnd[2] != 0.f)) alpha *= power_of_two(-static_cast<int>(bnd[2]));
       const bool moved = __any_sync(0xffffffffu, alpha != 1.f);
 
       // ---- weights as hi and lo bytes, a 16-byte unit of P's row, and their sum
@@ -551,35 +548,35 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
       next = w;
       int n = 0, m = 0;
       float bound = 1.f;
+      bool nothing = false;
       // The scales, times kFactorUnit (1 past the end, and for one that is 0 or not finite), kUnit scale / R (0 there), and
-      // log2(scale / R).  R is over the tokens that every row sees, and the first, which every row that sees one
-      // of the segment's tokens sees.  A row that sees a token whose scale is not finite gets a NaN score; to the
-      // others it is nothing.  Four slots: factors m + 4 are made once S(m + 3) is
-      // done, which waits until the softmax has left tile m.
+      // log2(scale / R).  A row that sees a token whose scale is not finite gets a NaN score; to the others it is nothing.
+      // Four slots: factors m + 4 are made once S(m + 3) is done, which waits until the softmax has left tile m.
       auto factors = [&]() {
         ok = warp_wait(bar(kScaleFull + (m & 3)), (m >> 2) & 1, abort_flag);
         if (!ok) return;
-        const int L = __ldg(P.cache_seqlens + next.i);
-        const int at = next.p * kPage + 4 * lane;
-        const int end = min(L, next.p_end * kPage) - at, all_see = P.causal ? min(end, L - P.s_q + 1 - at) : end;
+        const int L = __ldg(P.cache_seqlens + next.i), t0 = next.p * kPage, t = t0 + 4 * lane;
+        const int end = min(L, next.p_end * kPage), all_see = P.causal ? min(end, L - P.s_q + 1) : end;
+        const bool first = next.first();
         const float4 s4 = reinterpret_cast<const float4*>(gbase + kOffScale)[(m & 3) * 32 + lane];
         float s[4] = {s4.x, s4.y, s4.z, s4.w}, scale[4];
         bool odd = false;
-        uint32_t top = 0, any = 0;
+        uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool fine = s[e] > 0.f && s[e] < INFINITY;
-          odd = odd || (e < end && !fine);
-          scale[e] = e < end && fine ? fmaxf(s[e] * kFactorUnit, 0x1p-149f) : 1.f;
-          if (!(e < end && fine)) s[e] = 0.f;
-          any = max(any, __float_as_uint(s[e]));
-          if (e < all_see || 4 * lane + e == 0) top = max(top, __float_as_uint(s[e]));
+          const bool fine = t + e < end && s[e] > 0.f && s[e] < INFINITY;
+          odd = odd || (t + e < end && !fine);
+          scale[e] = fine ? fmaxf(s[e] * kFactorUnit, 0x1p-149f) : 1.f;
+          if (!fine) s[e] = 0.f;
+          if (t + e < all_see || (first && t + e == t0)) top = max(top, __float_as_uint(s[e]));
         }
         odd = __any_sync(0xffffffffu, odd);
         float shift = 0.f;
-        if (rare(next.first() || bound == kMinR)) {
-          const float r = reference_scale(__reduce_max_sync(0xffffffffu, top), __reduce_max_sync(0xffffffffu, any));
-          if (!next.first()) shift = static_cast<float>(log2_of_power(r) - log2_of_power(bound));
+        if (rare(first || (nothing && t0 < all_see))) {
+          top = __reduce_max_sync(0xffffffffu, top);
+          nothing = is_nothing(top);
+          const float r = reference_scale(top);
+          if (!first) shift = static_cast<float>(log2_of_power(r) - log2_of_power(bound));
           bound = r;
         }
         const float u = 1.f / bound;

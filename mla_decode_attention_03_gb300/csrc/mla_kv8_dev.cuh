@@ -19,12 +19,13 @@ constexpr int kTile = 128;  // tokens: two pages
 // see among them.  M is moved (and O rescaled, between two products) only when it
 // grew by more than kSlack (log2): weights stay below kUnit 2^kSlack < 448, e4m3's
 // largest.  R, a power of two, serves the range only: P and its sum l reach R / scale.
-// It is made from the segment's first tile, or, while there is nothing above kMinR, from
-// the first one that holds more (see move_reference).
 constexpr float kMargin = 1.f;             // a maximum that moves goes this far beyond, so that it moves less often
-constexpr float kMinR = 0x1p-60f, kMaxR = 0x1p40f;
-constexpr float kMaxRatio = 0x1p101f;      // of scale / R
-constexpr float kMinLog = -80.f;           // of its log2, as far as M goes; 0 has it too
+// R is about the largest scale of a segment's first tile, within limits between which both
+// ends of the scales' range are in reach: 2^-126 is 2^-100 of the lower, 2^128 2^98 of the upper.
+constexpr float kMinR = 0x1p-26f, kMaxR = 0x1p30f;
+constexpr float kMinLog = -100.f;          // of log2(scale / R), as far as M goes; 0 has it too: P is up to 2^100
+constexpr float kMaxRatio = 0x1p101f;      // of scale / R: a weight's P is 2^-101, and those beside it are held to 2^-25 of it
+constexpr float kNothing = 0x1p-60f;       // such scales are next to nothing; an entry of zeros is written with 2^-126
 
 __device__ __forceinline__ float log_ratio(float ratio) {
   float y;
@@ -35,22 +36,19 @@ __device__ __forceinline__ float log_ratio(float ratio) {
 __device__ __forceinline__ int log2_of_power(float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; }  // positive, normal
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // normal ones
 
-// R of a tile, from the bits of its largest finite scales: `top` over the tokens that every
-// row sees and the first one, which every row that sees one of the segment's sees; `any` over
-// all inside the sequence, some of which only some rows see.  Those count only where the
-// others have next to nothing, and as little as keeps them below kMaxRatio.
-__device__ __forceinline__ float reference_scale(uint32_t top, uint32_t any) {
-  float r = __uint_as_float(top & 0x7f800000u);  // the power of two at or below it
-  if (!(r > kMinR)) r = fmaxf(kMinR, __uint_as_float(any & 0x7f800000u) * 0x1p-100f);
-  return fminf(r, kMaxR);
+// R for tokens of which `top` is the largest finite scale, in bits; kMinR where that is nothing.
+//
+// These are the tokens that every row sees, for what a row does not see must not change
+// its bits; and a segment's first, which every row that sees one of them sees.  While they
+// hold nothing, R stays kMinR (rows that see more see scales up to 2^75 well), and moves once,
+// at the first tile that has more for every row.  O is in units of R; P, l and M stay: M, of
+// what was nothing, is 34 to 100 below its scores, low enough for what comes.
+__device__ __forceinline__ float reference_scale(uint32_t top) {
+  return fminf(fmaxf(__uint_as_float(top & 0x7f800000u), kMinR), kMaxR);
 }
+__device__ __forceinline__ bool is_nothing(uint32_t top) { return !(__uint_as_float(top) > kNothing); }
 
-// Where R moves from kMinR to a later tile's, what the rows have so far is of tokens of next
-// to no scale.  Their P and l do not change, O, in units of R, does, and M, in terms of
-// scale / R, may come down by as much: by kMaxLess at most, for l <= tokens * 2^80 grows by that.
-constexpr float kMaxLess = 24.f;
-
-// A move of M by d changes l by 2^d, which is made as the square of this: l may reach 2^80
+// A move of M by d changes l by 2^d, which is made as the square of this: l may reach 2^100
 // by tokens of no scale, and what is then left of it still counts although 2^d is below 2^-126.
 __device__ __forceinline__ float root_of_move(float d) { return ex2_approx(0.5f * d); }
 

@@ -142,3 +142,54 @@ def test_smallest_entries_keep_their_bits(h_q):
     for parts in (None, 1):
         out, lse = decode(*x, parts=parts)
         held(out, lse, (o, l, ob - 1e-30 + 2.0 ** -133, lb))
+
+
+@gpu
+@pytest.mark.parametrize("h_q,s_q", [(16, 3), (4, 5), (33, 3), (128, 3)])
+@pytest.mark.parametrize("kind", ["scale 0", "written zeros", "scale 2^-70"])
+def test_last_tokens_after_next_to_nothing(h_q, s_q, kind):
+    """Entries next to nothing but for the last ones, which only some queries see: each query has what it sees, and keeps
+    it, bit for bit, whatever the last one's scale is."""
+    lens = [129, 65, 128, 130, 193, 3, 64, 66]
+    q0, cache, scales0, bt, sl = inputs(lens, s_q, h_q, seed=63)
+    codes = cache.view(torch.uint8)
+    for i, L in enumerate(lens):
+        for t in range(max(0, L - s_q + 1)):
+            scales0[at(bt, i, t)] = {"scale 0": 0.0, "written zeros": 2.0 ** -126, "scale 2^-70": 2.0 ** -70}[kind]
+            if kind == "written zeros":
+                codes[int(bt[i, t // 64]), t % 64] = 0
+    for power in (0, -40, 30, 70):
+        scales = torch.where(scales0 > 2.0 ** -60, scales0 * 2.0 ** power, scales0)
+        for level in (1.0, 8.0):
+            q = (q0.float() * (level * 2.0 ** -power)).to(torch.bfloat16)
+            ref = attention(q, cache, scales, bt, sl, SCALE, True)
+            for parts in (None, 1, 2):
+                out, lse = decode(q, cache, scales, bt, sl, causal=True, parts=parts)
+                held(out, lse, ref)
+                for value in (0.0, 1.0, 3e38, math.nan):
+                    hidden = scales.clone()
+                    for i, L in enumerate(lens):
+                        hidden[at(bt, i, L - 1)] = value
+                    got = decode(q, cache, hidden, bt, sl, causal=True, parts=parts)
+                    assert torch.equal(got[0][:, :-1], out[:, :-1]) and torch.equal(got[1][..., :-1], lse[..., :-1]), value
+
+
+@gpu
+@pytest.mark.parametrize("h_q,s_q", [(16, 3), (33, 5), (128, 2)])
+def test_hidden_scales_beside_small_ones(h_q, s_q):
+    """Sequences of small entries: a hidden token's scale, as large as it may be, leaves the others' bits alone."""
+    lens = [128, 300, 129, 65, 1, 5]
+    q, cache, scales, bt, sl = inputs(lens, s_q, h_q, seed=64)
+    for power in (-100, -60, -30):
+        x = ((q.float() * 2.0 ** -power).to(torch.bfloat16), cache, scales * 2.0 ** power, bt, sl)
+        ref = attention(*x, SCALE, True)
+        for parts in (None, 1, 20):
+            out, lse = decode(*x, causal=True, parts=parts)
+            # (the reference's floor of 1e-30 is above these outputs; rows that see nothing have none)
+            held(out, lse, (ref[0], ref[1], (ref[2] - 1e-30).clamp(min=0) + 2.0 ** -133, ref[3]))
+            for value in (0.0, 1.0, 3e38):
+                hidden = x[2].clone()
+                for i, L in enumerate(lens):
+                    hidden[at(bt, i, L - 1)] = value
+                got = decode(x[0], cache, hidden, bt, sl, causal=True, parts=parts)
+                assert torch.equal(got[0][:, :-1], out[:, :-1]) and torch.equal(got[1][..., :-1], lse[..., :-1]), value
