@@ -177,7 +177,9 @@ mla_decode_kv8_pair_kernel(const __grid_constant__ CUtensorMap lat_map, const __
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + kOffMisc + 8);
 
   const int tid = threadIdx.x;
-  const int warp = tid >> 5;
+  // The same in all lanes, and by the shuffle the compiler knows it: branches on it are then uniform, and so are the
+  // operands of what is issued in them (128 heads, batch 128: 126.1 us a call; with tid >> 5 alone 132.4).
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int lane = tid & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int unit = blockIdx.x >> 1;
