@@ -29,13 +29,14 @@
 // A segment's queries, 73 KB as hi + lo, come from global memory in the form that
 // the MMAs read: mla_kv8_queries_kernel makes them once per call (a few warps of
 // each CTA, making them per segment, took 18,000 cycles a segment; as a kernel of
-// its own they take 5 us of the 125, and converting them in here, by warps that are
-// spare, at a segment's end or in place, 2 to 20 us more).
+// its own they take 5 us of the 126, and converting them in here, by warps that are
+// spare, at a segment's beginning or end or in place, 2 to 20 us more).
 //
 // Bound: the tensor cores' operand traffic (S reads 4 KB of shared memory per 32
 // cycles of MMA, all that there is) and a tile's residence of about 10,000 cycles
-// over the three that fit.  128 sequences of 4096 tokens, 128 heads: 125 us a call,
-// 1.17 PFLOP/s, the pipe busy 58% of this kernel's 114 us.
+// over the three that fit.  128 sequences of 4096 tokens, 128 heads: 126 us a call
+// (ten in a graph; 134 as the only one, L2 cold), 1.16 PFLOP/s, the pipe busy 56% of
+// this kernel's cycles.
 //
 // Warps (768 threads, one CTA per SM, 2 CTAs per cluster):
 //   0-15   softmax and epilogue

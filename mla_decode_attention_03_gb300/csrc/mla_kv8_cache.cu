@@ -1,9 +1,9 @@
 // Writing new tokens into the 8-bit latent cache, and reading ranges back.
 // Both move bytes once: bound by HBM bandwidth on long inputs and by launch
-// and load latency on a decode step's few tokens.  Measured: writing 128 tokens
-// 1.8 us, 16001 tokens to scattered slots 7.2 us (28 MB: 3.9 TB/s; two tokens a
-// warp were no faster); reading 262,000 tokens back 72.9 us (6.2 TB/s, 0.92 of
-// the copy rate).
+// and load latency on a decode step's few tokens.  Measured, of ten calls in a graph
+// (what is written then lies largely in L2): writing 128 tokens 2.0 us, 16001 tokens
+// to scattered slots 7.2 us (28 MB: 3.9 TB/s; two tokens a warp were no faster);
+// reading 262,000 tokens back 73 us (6.2 TB/s, 0.91 of the copy rate).
 #include <cstdint>
 
 #include "mla_kv8_internal.h"

@@ -5,9 +5,9 @@
 //
 // Bound by the chain of its loads (pieces' bounds, then lse and values together,
 // then the store) and by cold code on small batches, by L2 on large ones.  Its part
-// of a call: 16 heads, 16 sequences in ten pieces each 4.5 us (256 rows, 5 MB); 60
-// rows, 37 sequences 3.7 (6.3 with the merge of the bf16 decode); 128 heads, 128
-// sequences, most in two pieces 5.9 (57 MB).
+// of a call (ten in a graph): 16 heads, 16 sequences in ten pieces each 4.5 us (256
+// rows, 5 MB); 60 rows, 37 sequences 3.7 (6.3 with the merge of the bf16 decode); 128
+// heads, 128 sequences, most in two pieces 5.9 (57 MB).
 #include <cuda_bf16.h>
 
 #include "mla_kv8_internal.h"
