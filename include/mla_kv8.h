@@ -88,8 +88,8 @@ mla_status_t mla_read_cache_kv8(const void *codes, const float *scales, int64_t 
  * the scales of a sequence that are above 2^-60 lie within 2^80 of one another (smaller
  * ones beside them, those of zero entries among them, count in full in the softmax);
  * where all that every query sees is at or below 2^-60, what only some see may be up to
- * 2^75.  For more than 262140
- * rows s_q h_q, which no decode takes, the two sizes are MLA_ERR_UNSUPPORTED and 0.
+ * 2^75.  For more than 262140 rows s_q h_q, which no decode takes, the part count is
+ * MLA_ERR_UNSUPPORTED and the workspace size 0.
  */
 int mla_num_parts_kv8(int s_q, int h_q, int h_kv, int device);
 
