@@ -12,7 +12,6 @@ import ctypes
 import functools
 import math
 import threading
-from fractions import Fraction
 from pathlib import Path
 
 import torch
@@ -685,7 +684,9 @@ def _pi() -> int:
 
 def _turns(f: float) -> int:
     """f radians as turns in 64-bit fixed point, whole turns dropped, rounded once."""
-    return round(Fraction(f) * (1 << (_PI_BITS + 63)) / _pi()) % (1 << 64)
+    num, den = f.as_integer_ratio()
+    den *= _pi()
+    return ((num << (_PI_BITS + 64)) + den) // (2 * den) % (1 << 64)
 
 
 class Rotary:
